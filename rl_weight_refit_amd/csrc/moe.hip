@@ -220,6 +220,8 @@ __device__ __forceinline__ float score32(float x, float m, float rz, bool sigmoi
 template <int RUN>
 __global__ __launch_bounds__(256) void rs_route_kernel(RouteArgs p) {
   constexpr uint32_t kPlace = RUN - 1;  // the key bits that hold the place in the run
+  constexpr int kPlaceBits = RUN > 64 ? 7 : 6;
+  constexpr uint32_t kExpert = (16u << kPlaceBits) - 1;  // those that hold lane and place
   const int lane = threadIdx.x & 15;
   const int64_t t = int64_t(blockIdx.x) * 16 + (threadIdx.x >> 4);
   const bool live = t < p.n_tokens && !(p.mask && !p.mask[t]);
@@ -308,15 +310,16 @@ __global__ __launch_bounds__(256) void rs_route_kernel(RouteArgs p) {
 
   // Keys; those up to kNone, -infinity's, are no candidates.
   constexpr uint32_t kNone = 0x007FFFFFu;
-  bool whole = false;  // logits of at most 13 mantissa bits: room for the lane too
+  bool whole = false;  // logits of at most 13 (12) mantissa bits: room for the lane too
   if (p.by_logit) {
     uint32_t low = 0;
 #pragma unroll
-    for (int j = 0; j < RUN; ++j) low |= __float_as_uint(v[j]) & 0x3FFu;
+    for (int j = 0; j < RUN; ++j) low |= __float_as_uint(v[j]) & kExpert;
     whole = row_max16u(low) == 0;
   }
   uint32_t key[RUN];
-  const uint32_t keep = !on ? 0u : whole ? ~0x3FFu : ~kPlace, tag = whole ? uint32_t(15 - lane) << 6 : 0u;
+  const uint32_t keep = !on ? 0u : whole ? ~kExpert : ~kPlace;
+  const uint32_t tag = whole ? uint32_t(15 - lane) << kPlaceBits : 0u;
 #pragma unroll
   for (int j = 0; j < RUN; ++j) key[j] = (key_of(v[j]) & keep) | (kPlace - j);
   if (p.by_logit) {
@@ -907,13 +910,32 @@ __global__ __launch_bounds__(256) void rs_combine_grad_kernel(CombineGradArgs p)
 
 }  // namespace
 
+// The lanes that one of n_groups groups takes, as a power of two.
+constexpr int route_lanes_shift(int n_groups) {
+  int shift = 4;
+  for (int slots = 1; slots < n_groups; slots <<= 1) --shift;
+  return shift;
+}
+// The most experts that a lane can hold: 113, of 1,017 in nine groups.  (Runs
+// above 64, which take large groups whose number is no power of two, keep part
+// of their values in scratch memory: 65,536 tokens of 1,000 experts in ten
+// groups 650 us, of 1,024 in eight 153.)
+constexpr int longest_run() {
+  int most = 0;
+  for (int g = 1; g <= kMaxRouteGroups; ++g) {
+    const int size = kMaxExperts / g, run = (size + (1 << route_lanes_shift(g)) - 1) >> route_lanes_shift(g);
+    if (run > most) most = run;
+  }
+  return most;
+}
+static_assert(longest_run() <= 128, "a kernel for every router");
+
 hipError_t launch_route(const rs_router& r, int64_t n_tokens, const void* logits, int64_t stride,
                         const float* bias, const uint8_t* mask, int32_t* ids, float* weights,
                         hipStream_t stream) {
   RouteArgs p{logits, bias, mask, ids, weights, n_tokens, stride, r.n_experts, r.top_k, r.n_groups,
               r.top_groups, r.group_top, r.renormalise, r.score == RS_SCORE_SIGMOID, r.logits_dtype,
-              r.n_experts / r.n_groups, 4, 0, 0, r.scale};
-  for (int slots = 1; slots < r.n_groups; slots <<= 1) --p.lanes_shift;
+              r.n_experts / r.n_groups, route_lanes_shift(r.n_groups), 0, 0, r.scale};
   p.run = (p.group_size + (1 << p.lanes_shift) - 1) >> p.lanes_shift;
   p.by_logit = !bias && (r.n_groups == 1 || r.group_top == 1 || p.group_size == 1);
   const dim3 grid(uint32_t((n_tokens + 15) / 16));
@@ -921,7 +943,8 @@ hipError_t launch_route(const rs_router& r, int64_t n_tokens, const void* logits
   else if (p.run <= 8) rs_route_kernel<8><<<grid, 256, 0, stream>>>(p);
   else if (p.run <= 16) rs_route_kernel<16><<<grid, 256, 0, stream>>>(p);
   else if (p.run <= 32) rs_route_kernel<32><<<grid, 256, 0, stream>>>(p);
-  else rs_route_kernel<64><<<grid, 256, 0, stream>>>(p);
+  else if (p.run <= 64) rs_route_kernel<64><<<grid, 256, 0, stream>>>(p);
+  else rs_route_kernel<128><<<grid, 256, 0, stream>>>(p);
   return hipGetLastError();
 }
 

@@ -353,3 +353,38 @@ def test_combine_grad_against_differences():
         up[r, c] += 1.0
         want = (H.combine(up, p, ww)[0] * dd).sum() - base
         assert abs(f64(dy)[r, c] - want) <= 8 * U32 + 1e-12 * abs(base)
+
+
+# Groups whose experts do not divide evenly over a token's lanes: runs of up to 113 experts a lane.
+WIDE_GROUPS = [(900, 9), (1020, 5), (1020, 6), (1000, 10), (771, 3), (585, 9), (1017, 9), (1023, 11), (1020, 12), (1014, 13),
+               (1022, 14), (1020, 15), (1022, 7)]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G", WIDE_GROUPS)
+def test_route_wide_groups(E, G, score):
+    for dtype, biased, group_top, k in (("f32", True, 2, 8), ("f32", False, 2, 8), ("bf16", False, 1, 8), ("f16", True, 1, 17),
+                                        ("f32", False, 1, 32)):
+        x = logits_for(14, E, dtype, E + k)
+        bias = (torch.randn(E, generator=torch.Generator().manual_seed(G)) * 0.05).cuda() if biased else None
+        x[1, ::3] = -float("inf")
+        x[2, : E - E // G] = float("nan")
+        x[3] = 0.0   # all alike: the lowest groups and experts
+        for renorm in (True, False):
+            check_route(x, dict(k=k, score=score, renorm=renorm, groups=G, top_groups=(G + 1) // 2, group_top=group_top), bias,
+                        dtype=dtype)
+
+
+@pytest.mark.parametrize("E,G", [(900, 9), (771, 3)])
+def test_route_wide_groups_take_the_last_experts(E, G):
+    """Every expert of a group can be chosen, the last ones of a run too; near
+    scores are told apart beyond float32."""
+    x = torch.full((E, E), -3.0)
+    x[torch.arange(E), torch.arange(E)] = 2.0
+    x[torch.arange(E), (torch.arange(E) + E // G - 1) % E] = 1.0
+    check_route(x.cuda(), dict(k=2, score="sigmoid", renorm=True, groups=G, top_groups=2))
+    rng = np.random.default_rng(0)
+    y = torch.tensor(rng.normal(0, 1, (40, E)), dtype=torch.float32)
+    y[:, 1::2] = torch.nextafter(y[:, :-1:2], torch.full_like(y[:, :-1:2], 9.0))[:, : y[:, 1::2].shape[1]]
+    for score in ("softmax", "sigmoid"):
+        check_route(y.cuda(), dict(k=8, score=score, renorm=False, groups=G, top_groups=2, group_top=2), torch.full((E,), 0.4).cuda())
