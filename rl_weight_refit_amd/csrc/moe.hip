@@ -205,16 +205,25 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 // instruction), the sum by 28 (its terms, weighted, and a tree of additions),
 // quotient and reciprocal by 4, and d is at most -log s: below
 // s (17 - log s) 2^-23.  Sigmoid: exp as before, but only s (1 - s) of it
-// arrives, below 0.7 units; the addition and the reciprocal (one unit of the
-// instruction, 2^-23) leave below 2^-23 (0.35 + 1.5 s).  And v's own rounding.
+// arrives, below 0.8 units; the addition and the reciprocal (one unit of the
+// instruction, 2^-23) leave below 2^-23 (0.4 + 1.5 s).  And v's own rounding.
 __device__ __forceinline__ float error_of(float s, float v, bool sigmoid) {
   const float f = sigmoid ? 0.5f + 1.5f * s : s * (17.0f - __logf(s + 1e-30f));
   return 0x1p-23f * (f + fabsf(v));
 }
 
+// The sigmoid and what is left of it to 1, both to a few units of themselves.
+struct Sigmoid {
+  float s, rest;
+};
+__device__ __forceinline__ Sigmoid sigmoid32(float x) {
+  const float e = expf(-fabsf(x)), r = 1.0f / (1.0f + e);
+  return x < 0.0f ? Sigmoid{e * r, r} : Sigmoid{r, e * r};
+}
+
 __device__ __forceinline__ float score32(float x, float m, float rz, bool sigmoid) {
   if (!(x > -INFINITY)) return 0.0f;
-  return sigmoid ? 1.0f / (1.0f + expf(-x)) : (x == m ? 1.0f : expf(x - m)) * rz;
+  return sigmoid ? sigmoid32(x).s : (x == m ? 1.0f : expf(x - m)) * rz;
 }
 
 template <int RUN>
@@ -473,8 +482,9 @@ __global__ __launch_bounds__(256) void rs_route_kernel(RouteArgs p) {
 // the others h_j = g_j; then dl_e = s_e (H_e - sum_j h_j p_j) for the softmax
 // and s_e (1 - s_e) H_e for the sigmoid, H_e being the sum of h_j over the
 // slots that name e.  Sixteen lanes a token, a run of experts and one or two
-// slots a lane; H goes through LDS, each expert written by the first slot
-// that names it with the sum of all that do, in slot order.
+// slots a lane; H (the sigmoid's with its factor) goes through LDS, each
+// expert written by the first slot that names it with the sum of all that do,
+// in slot order.
 struct RouteGradArgs {
   const void* logits;
   const int32_t* ids;
@@ -496,11 +506,12 @@ __global__ __launch_bounds__(RUN > 16 ? 64 : 256) void rs_route_grad_kernel(Rout
   const int64_t row = live ? t * p.stride : 0;
   const int first = lane * p.run;
   const int held = live ? max(0, min(p.run, p.n_experts - first)) : 0;
-  float x[RUN], s[RUN];
-  load_run<RUN>(p.logits, p.dtype, row + first, held, x);
-  nan_to_lowest(x);
+  float s[RUN];
   float m = 0.0f, z = 1.0f;
   if (!p.sigmoid) {
+    float x[RUN];
+    load_run<RUN>(p.logits, p.dtype, row + first, held, x);
+    nan_to_lowest(x);
     m = x[0];
 #pragma unroll
     for (int j = 1; j < RUN; ++j) m = fmaxf(m, x[j]);
@@ -516,21 +527,19 @@ __global__ __launch_bounds__(RUN > 16 ? 64 : 256) void rs_route_grad_kernel(Rout
 #pragma unroll
     for (int j = 0; j < RUN; ++j) s[j] *= rz;
     z = rz;
-  } else {
-#pragma unroll
-    for (int j = 0; j < RUN; ++j) s[j] = x[j] > -INFINITY ? 1.0f / (1.0f + expf(-x[j])) : 0.0f;
   }
   int32_t id[2];
-  float q[2], h[2];
+  float q[2], h[2], slope[2];   // slope: the sigmoid's s (1 - s)
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
     const int i = a * 16 + lane;
     id[a] = live && i < p.top_k ? p.ids[t * p.top_k + i] : -1;
     if (id[a] < 0 || id[a] >= p.n_experts) id[a] = -1;
-    q[a] = 0.0f;
+    q[a] = slope[a] = 0.0f;
     if (id[a] >= 0) {
       const float l = load1(p.logits, p.dtype, row + id[a]);
       q[a] = score32(l, m, z, p.sigmoid);
+      if (p.sigmoid && q[a] > 0.0f) slope[a] = q[a] * sigmoid32(l).rest;
     }
     h[a] = id[a] < 0 ? 0.0f : p.scale * p.dweights[t * p.top_k + i];
   }
@@ -541,6 +550,7 @@ __global__ __launch_bounds__(RUN > 16 ? 64 : 256) void rs_route_grad_kernel(Rout
     for (int a = 0; a < 2; ++a) h[a] = id[a] >= 0 && zs > 0.0f ? (h[a] - gp / zs) / zs : 0.0f;
   }
   const float mean = p.sigmoid ? 0.0f : row_sum16f(h[0] * q[0] + h[1] * q[1]);
+  if (p.sigmoid) h[0] *= slope[0], h[1] *= slope[1];
   float* mine = turn + (threadIdx.x >> 4) * kPitch;
 #pragma unroll
   for (int j = 0; j < RUN; ++j) mine[lane + 16 * j] = 0.0f;
@@ -565,8 +575,7 @@ __global__ __launch_bounds__(RUN > 16 ? 64 : 256) void rs_route_grad_kernel(Rout
 #pragma unroll
   for (int j = 0; j < RUN; ++j) {
     const float H = mine[lane * RUN + j];
-    const float d = p.sigmoid ? s[j] * (1.0f - s[j]) * H : s[j] * (H - mean);
-    s[j] = s[j] > 0.0f ? d : 0.0f;
+    s[j] = p.sigmoid ? H : s[j] > 0.0f ? s[j] * (H - mean) : 0.0f;
   }
   const int64_t to = t * p.dstride + first;
   if (RUN % 8 == 0 && held == RUN) {

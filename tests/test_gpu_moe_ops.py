@@ -388,3 +388,38 @@ def test_route_wide_groups_take_the_last_experts(E, G):
     y[:, 1::2] = torch.nextafter(y[:, :-1:2], torch.full_like(y[:, :-1:2], 9.0))[:, : y[:, 1::2].shape[1]]
     for score in ("softmax", "sigmoid"):
         check_route(y.cuda(), dict(k=8, score=score, renorm=False, groups=G, top_groups=2, group_top=2), torch.full((E,), 0.4).cuda())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_grad_of_saturated_sigmoids(dtype, renorm):
+    """s (1 - s) keeps its digits where s is next to 1 as where it is next to
+    0: e^-|l| / (1 + e^-|l|)^2 is off by 2 U from exp, the sum and the
+    quotients by less than 8 U together, three products by 3 U; the
+    renormalised weights' share (a second score, a sum over four slots, a
+    quotient, the difference) by less than 40 U of the magnitudes subtracted."""
+    x = torch.linspace(-80, 80, 64).repeat(16, 1)
+    x[1::2] = torch.linspace(10, 40, 64)
+    x = x.to(DT[dtype]).cuda()
+    rng = np.random.default_rng(1)
+    ids = np.stack([rng.permutation(64)[:4] for _ in range(16)]).astype(np.int32)
+    ids[2] = [63, 60, 60, 62]
+    g = rng.normal(0, 1, (16, 4)).astype(np.float32)
+    r = B.Router(dtype, 64, 4, score="sigmoid", renormalise=renorm, scale=1.5)
+    out = torch.full((16, 64), 7.0, dtype=DT[dtype], device="cuda")
+    B.reshard_moe_route_grad(r, 16, ptr(x), 64, ptr(torch.from_numpy(ids).cuda()), ptr(torch.from_numpy(g).cuda()),
+                             ptr(out), 64, stream())
+    xx, want, tol = f64(x), np.zeros((16, 64)), np.zeros((16, 64))
+    e = np.exp(-np.abs(xx))
+    s, rest = np.where(xx >= 0, 1, e) / (1 + e), np.where(xx >= 0, e, 1) / (1 + e)   # rest = 1 - s
+    for t in range(16):
+        p = s[t, ids[t]]
+        h = 1.5 * g[t].astype(np.float64)
+        a = np.abs(h)
+        if renorm:
+            h, a = (h - (h * p).sum() / p.sum()) / p.sum(), (a + (a * p).sum() / p.sum()) / p.sum()
+        for j in range(4):
+            i = ids[t, j]
+            want[t, i] += s[t, i] * rest[t, i] * h[j]
+            tol[t, i] += s[t, i] * rest[t, i] * a[j] * (64 if renorm else 24) * H.U
+    H.close(f64(out), want, tol, dtype, "dlogits")
