@@ -392,7 +392,9 @@ typedef struct rs_router {
  * their experts are chosen, in descending order; equal values go to the
  * lower group and the lower expert.  ids[t * top_k + j] receives expert j of
  * token t, weights[...] = scale * s_id, divided by the sum of the chosen s
- * where renormalise is 1 (all 0 where that sum is 0).
+ * where renormalise is 1 (all 0 where that sum is 0 in double precision:
+ * chosen logits all below -745, or as far below the token's largest for the
+ * softmax).
  * The choice is the one of exact arithmetic on the given logits and bias to
  * within double precision: scores that differ only beyond float32 are still
  * told apart.  Experts with +infinity logits share a softmax equally.  An

@@ -226,6 +226,27 @@ __device__ __forceinline__ float score32(float x, float m, float rz, bool sigmoi
   return sigmoid ? sigmoid32(x).s : (x == m ? 1.0f : expf(x - m)) * rz;
 }
 
+// Renormalised weights: the slots' scores are taken relative to the largest
+// one's, so that their quotients keep their digits where the scores themselves
+// lie below 2^-126.  `top` is the largest of the slots' logits, m the token's
+// largest (softmax).  kZero: where double precision has 0 for every score, all
+// weights are 0.
+struct Share {
+  float base;
+  bool none;
+};
+__device__ __forceinline__ Share share_base(float top, float m, bool sigmoid) {
+  constexpr float kZero = 745.0f;  // e^-745.13 is half of the smallest number
+  if (sigmoid) return Share{fminf(top, 0.0f), !(top >= -kZero)};
+  return Share{top, !(top > -INFINITY) || (top != m && !(m - top <= kZero))};
+}
+__device__ __forceinline__ float share32(float x, const Share& b, bool sigmoid) {
+  if (b.none || !(x > -INFINITY)) return 0.0f;
+  const float e = x == b.base ? 1.0f : expf(x - b.base);
+  if (!sigmoid) return e;
+  return x < 0.0f ? e / (1.0f + expf(x)) : 1.0f / (1.0f + expf(-x));
+}
+
 template <int RUN>
 __global__ __launch_bounds__(256) void rs_route_kernel(RouteArgs p) {
   constexpr uint32_t kPlace = RUN - 1;  // the key bits that hold the place in the run
@@ -361,9 +382,7 @@ __global__ __launch_bounds__(256) void rs_route_kernel(RouteArgs p) {
     const int place = int(kPlace - (key_at & kPlace)), from = __ffs(int(won_at >> (threadIdx.x & 16) & 0xFFFFu)) - 1;
     return (from >> p.lanes_shift) * p.group_size + (from & ((1 << p.lanes_shift) - 1)) * p.run + place;
   };
-  const auto score_of = [&](int e) {
-    return e < 0 ? 0.0f : score32(load1(p.logits, p.dtype, t * p.stride + e), m, rz, p.sigmoid);
-  };
+  const auto logit_of = [&](int e) { return e < 0 ? -INFINITY : load1(p.logits, p.dtype, t * p.stride + e); };
   // The most that a slot's value can exactly be (a key's value is short of
   // the float32 one by less than RUN steps), and the least.
   const auto most = [&](uint32_t k, float score) {
@@ -379,12 +398,16 @@ __global__ __launch_bounds__(256) void rs_route_kernel(RouteArgs p) {
     for (int i = 0; i < 16 && h * 16 + i <= p.top_k; ++i) pick(i, chosen[h], winner[h]);
   // Expert and score of each lane's slots, the one beyond the last among them.
   int32_t slot[3] = {-1, -1, -1};
-  float s[3] = {0.0f, 0.0f, 0.0f};
+  float logit[3] = {-INFINITY, -INFINITY, -INFINITY}, s[3] = {0.0f, 0.0f, 0.0f};
+  const auto take = [&](int h, int e) {
+    slot[h] = e;
+    logit[h] = logit_of(e);
+    s[h] = score32(logit[h], m, rz, p.sigmoid);
+  };
 #pragma unroll
   for (int h = 0; h < 3; ++h) {
     if (h * 16 > p.top_k) continue;
-    slot[h] = expert_of(chosen[h], winner[h]);
-    s[h] = score_of(slot[h]);
+    take(h, expert_of(chosen[h], winner[h]));
   }
   // Each slot against the next: in order if the values lie further apart than
   // both can be off.
@@ -410,7 +433,7 @@ __global__ __launch_bounds__(256) void rs_route_kernel(RouteArgs p) {
     // sixteenth; if that may reach the last slot, the token stays open.
     for (int i = p.top_k + 1; i < 16; ++i) pick(i, chosen[0], winner[0]);
     const int e = expert_of(chosen[0], winner[0]);
-    const float l = e >= 0 ? load1(p.logits, p.dtype, t * p.stride + e) : -INFINITY;
+    const float l = logit_of(e);
     double v64 = -INFINITY;
     if (p.by_logit) {
       if (e >= 0) v64 = !p.sigmoid && m == INFINITY && l < m ? 0.0 : double(l);
@@ -427,7 +450,7 @@ __global__ __launch_bounds__(256) void rs_route_kernel(RouteArgs p) {
       }
       if (e >= 0) v64 = score64(l, m, z, p.sigmoid) + (p.bias ? double(p.bias[e]) : 0.0);
     }
-    const float beyond = __shfl(most(chosen[0], score_of(e)), 15, 16);
+    const float beyond = __shfl(most(chosen[0], score32(l, m, rz, p.sigmoid)), 15, 16);
     int rank = 0;
     for (int j = 0; j < 16; ++j) {
       const double o = __shfl(v64, j, 16);
@@ -442,8 +465,7 @@ __global__ __launch_bounds__(256) void rs_route_kernel(RouteArgs p) {
     }
     if (close && row_any(!sure)) open = true;
     if (close && held_off && !open) {
-      slot[0] = sorted;
-      s[0] = score_of(sorted);
+      take(0, sorted);
       close = false;
     }
   }
@@ -452,39 +474,40 @@ __global__ __launch_bounds__(256) void rs_route_kernel(RouteArgs p) {
     int32_t again[2];
     choose64<RUN>(p, t, lane, group, first, held, again);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      slot[h] = again[h];
-      s[h] = score_of(slot[h]);
-    }
+    for (int h = 0; h < 2; ++h) take(h, again[h]);
   }
 
   if (t >= p.n_tokens) return;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    if (h * 16 + lane >= p.top_k) slot[h] = -1, s[h] = 0.0f;
-  float f = p.scale;
+    if (h * 16 + lane >= p.top_k) slot[h] = -1, logit[h] = -INFINITY, s[h] = 0.0f;
   if (p.renormalise) {
+    const Share base = share_base(row_max16f(fmaxf(logit[0], logit[1])), m, p.sigmoid);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) s[h] = share32(logit[h], base, p.sigmoid);
     const float sum = row_sum16f(s[0] + s[1]);
-    f = sum > 0.0f ? f / sum : 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) s[h] = sum > 0.0f ? s[h] / sum : 0.0f;
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int i = h * 16 + lane;
     if (i < p.top_k) {
       p.ids[t * p.top_k + i] = slot[h];
-      p.weights[t * p.top_k + i] = s[h] * f;
+      p.weights[t * p.top_k + i] = s[h] * p.scale;
     }
   }
 }
 
-// Gradient of the weights: with g_j = scale * dweights_j, p_j = s at slot j
-// and Z = sum p, the renormalised weights give h_j = (g_j - sum g p / Z) / Z,
-// the others h_j = g_j; then dl_e = s_e (H_e - sum_j h_j p_j) for the softmax
-// and s_e (1 - s_e) H_e for the sigmoid, H_e being the sum of h_j over the
-// slots that name e.  Sixteen lanes a token, a run of experts and one or two
-// slots a lane; H (the sigmoid's with its factor) goes through LDS, each
-// expert written by the first slot that names it with the sum of all that do,
-// in slot order.
+// Gradient of the weights, with g_j = scale * dweights_j and p_j = s at slot
+// j.  dl_e = s_e (H_e - sum_j g_j p_j) for the softmax and s_e (1 - s_e) H_e
+// for the sigmoid, H_e being the sum of g_j over the slots that name e.
+// Renormalised weights, with their shares r_j = p_j / sum p: dl_e is the sum of
+// r_j (g_j - sum g r) over the slots that name e (the softmax's sum over all
+// slots is 0), times 1 - s_e for the sigmoid.  Sixteen lanes a token, a run of
+// experts and one or two slots a lane; H (what is not the softmax's own, with
+// its factors: dl_e itself) goes through LDS, each expert written by the first
+// slot that names it with the sum of all that do, in slot order.
 struct RouteGradArgs {
   const void* logits;
   const int32_t* ids;
@@ -529,28 +552,37 @@ __global__ __launch_bounds__(RUN > 16 ? 64 : 256) void rs_route_grad_kernel(Rout
     z = rz;
   }
   int32_t id[2];
-  float q[2], h[2], slope[2];   // slope: the sigmoid's s (1 - s)
+  float l[2], q[2], h[2];
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
     const int i = a * 16 + lane;
     id[a] = live && i < p.top_k ? p.ids[t * p.top_k + i] : -1;
     if (id[a] < 0 || id[a] >= p.n_experts) id[a] = -1;
-    q[a] = slope[a] = 0.0f;
-    if (id[a] >= 0) {
-      const float l = load1(p.logits, p.dtype, row + id[a]);
-      q[a] = score32(l, m, z, p.sigmoid);
-      if (p.sigmoid && q[a] > 0.0f) slope[a] = q[a] * sigmoid32(l).rest;
-    }
+    l[a] = id[a] < 0 ? -INFINITY : load1(p.logits, p.dtype, row + id[a]);
+    l[a] = l[a] == l[a] ? l[a] : -INFINITY;
     h[a] = id[a] < 0 ? 0.0f : p.scale * p.dweights[t * p.top_k + i];
   }
+  float mean = 0.0f;
   if (p.renormalise) {
-    const float zs = row_sum16f(q[0] + q[1]);
-    const float gp = row_sum16f(h[0] * q[0] + h[1] * q[1]);
+    const Share base = share_base(row_max16f(fmaxf(l[0], l[1])), m, p.sigmoid);
 #pragma unroll
-    for (int a = 0; a < 2; ++a) h[a] = id[a] >= 0 && zs > 0.0f ? (h[a] - gp / zs) / zs : 0.0f;
+    for (int a = 0; a < 2; ++a) q[a] = share32(l[a], base, p.sigmoid);
+    const float sum = row_sum16f(q[0] + q[1]);
+#pragma unroll
+    for (int a = 0; a < 2; ++a) q[a] = sum > 0.0f ? q[a] / sum : 0.0f;
+    const float gr = row_sum16f(h[0] * q[0] + h[1] * q[1]);
+#pragma unroll
+    for (int a = 0; a < 2; ++a) h[a] = q[a] * (h[a] - gr);
+  } else {
+#pragma unroll
+    for (int a = 0; a < 2; ++a) q[a] = score32(l[a], m, z, p.sigmoid);
+    if (!p.sigmoid) mean = row_sum16f(h[0] * q[0] + h[1] * q[1]);
+    else h[0] *= q[0], h[1] *= q[1];
   }
-  const float mean = p.sigmoid ? 0.0f : row_sum16f(h[0] * q[0] + h[1] * q[1]);
-  if (p.sigmoid) h[0] *= slope[0], h[1] *= slope[1];
+  if (p.sigmoid) {
+#pragma unroll
+    for (int a = 0; a < 2; ++a) h[a] = l[a] > -INFINITY ? h[a] * sigmoid32(l[a]).rest : 0.0f;
+  }
   float* mine = turn + (threadIdx.x >> 4) * kPitch;
 #pragma unroll
   for (int j = 0; j < RUN; ++j) mine[lane + 16 * j] = 0.0f;
@@ -575,7 +607,7 @@ __global__ __launch_bounds__(RUN > 16 ? 64 : 256) void rs_route_grad_kernel(Rout
 #pragma unroll
   for (int j = 0; j < RUN; ++j) {
     const float H = mine[lane * RUN + j];
-    s[j] = p.sigmoid ? H : s[j] > 0.0f ? s[j] * (H - mean) : 0.0f;
+    s[j] = p.sigmoid || p.renormalise ? H : s[j] > 0.0f ? s[j] * (H - mean) : 0.0f;
   }
   const int64_t to = t * p.dstride + first;
   if (RUN % 8 == 0 && held == RUN) {

@@ -423,3 +423,52 @@ def test_route_grad_of_saturated_sigmoids(dtype, renorm):
             want[t, i] += s[t, i] * rest[t, i] * h[j]
             tol[t, i] += s[t, i] * rest[t, i] * a[j] * (64 if renorm else 24) * H.U
     H.close(f64(out), want, tol, dtype, "dlogits")
+
+
+def tiny_scores(score):
+    """Logits and a bias that forces the choice of experts whose scores lie
+    below the smallest normal float32 number, or below any."""
+    x = torch.full((8, 16), 0.0)
+    if score == "softmax":
+        for t, d in enumerate((80.0, 95.0, 100.0, 110.0, 200.0, 600.0, 0.0, 30.0)):
+            x[t, 8:] = d
+    else:
+        for t, d in enumerate((80.0, 88.5, 95.0, 100.0, 110.0, 200.0, 600.0, -3.0)):
+            x[t, :8] = -d
+    x[:, :8] += torch.linspace(-2, 2, 8)
+    return x, torch.where(torch.arange(16) < 8, 2.0, 0.0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k", [1, 4])
+def test_route_renormalises_tiny_scores(score, k):
+    x, bias = tiny_scores(score)
+    for scale in (1.0, 2.5):
+        check_route(x.cuda(), dict(k=k, score=score, renorm=True, scale=scale), bias.cuda())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_no_weight_where_the_scores_are_zero(score):
+    """Sums that are 0 in double precision: logits below -745, next to one 800 or infinitely higher."""
+    x, bias = tiny_scores(score)
+    if score == "softmax":
+        x[0, 8:], x[1, 8:], x[2, 8:] = 800.0, float("inf"), torch.finfo(torch.float32).max
+    else:
+        x[0, :8], x[1, :8], x[2, :8] = -800.0, -1e30, torch.finfo(torch.float32).min
+    ids, w = run_route(x.cuda(), dict(k=3, score=score, renorm=True), bias.cuda())
+    assert (w[:3] == 0).all() and (w[3:] > 0).all() and (ids < 8).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k", [1, 3])
+def test_route_grad_of_tiny_scores(score, k):
+    x, _ = tiny_scores(score)
+    rng = np.random.default_rng(k)
+    ids = np.stack([rng.permutation(8)[:k] for _ in range(8)]).astype(np.int32)
+    g = rng.normal(0, 1, (8, k)).astype(np.float32)
+    r = B.Router("f32", 16, k, score=score, renormalise=True, scale=2.0)
+    out = torch.full((8, 16), 7.0, device="cuda")
+    B.reshard_moe_route_grad(r, 8, ptr(x.cuda()), 16, ptr(torch.from_numpy(ids).cuda()), ptr(torch.from_numpy(g).cuda()),
+                             ptr(out), 16, stream())
+    want, tol = H.route_grad(f64(x), ids, g.astype(np.float64), dict(score=score, renorm=True, scale=2.0))
+    H.close(f64(out), want, tol, "f32", "dlogits")
