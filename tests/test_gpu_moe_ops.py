@@ -472,3 +472,16 @@ def test_route_grad_of_tiny_scores(score, k):
                              ptr(out), 16, stream())
     want, tol = H.route_grad(f64(x), ids, g.astype(np.float64), dict(score=score, renorm=True, scale=2.0))
     H.close(f64(out), want, tol, "f32", "dlogits")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_token_does_not_depend_on_its_neighbours(score):
+    """Ordinary tokens, tiny scores and equal ones in one wave give the bytes that each gives alone."""
+    x, bias = tiny_scores(score)
+    x = torch.cat([x, logits_for(29, 16, "f32", 5).cpu(), torch.zeros(3, 16)])[torch.randperm(40, generator=torch.Generator().manual_seed(0))]
+    x, bias = x.cuda(), bias.cuda()
+    c = dict(k=3, score=score, renorm=True)
+    ids, w = run_route(x, c, bias)
+    for t in range(40):
+        i, v = run_route(x[t:t + 1], c, bias)
+        assert torch.equal(ids[t:t + 1], i) and torch.equal(w[t:t + 1].view(torch.int32), v.view(torch.int32))
