@@ -398,7 +398,7 @@ typedef struct rs_router {
  * The choice is the one of exact arithmetic on the given logits and bias to
  * within double precision: scores that differ only beyond float32 are still
  * told apart.  Experts with +infinity logits share a softmax equally.  An
- * expert whose logit is NaN or -infinity is never chosen (a
+ * expert whose logit or bias is NaN or -infinity is never chosen (a
  * group short of group_top others scores -infinity); slots left without an
  * expert get id -1 and weight 0.  token_mask (optional): one byte per token;
  * a token whose byte is 0 (padding) gets id -1 and weight 0 throughout. */

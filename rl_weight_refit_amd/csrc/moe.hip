@@ -146,6 +146,7 @@ __device__ __forceinline__ void choose64(const RouteArgs& p, int64_t t, int lane
     if (!(x[j] > -INFINITY)) v[j] = -INFINITY;
     else if (p.by_logit) v[j] = !p.sigmoid && m == INFINITY && x[j] < m ? 0.0 : double(x[j]);
     else v[j] = score64(x[j], m, z, p.sigmoid) + (p.bias ? double(p.bias[first + j]) : 0.0);
+    if (v[j] != v[j]) v[j] = -INFINITY;  // the bias is NaN
   }
   if (p.n_groups > 1) {
     double a = -INFINITY, b = -INFINITY;  // the two largest values of the group
@@ -293,11 +294,21 @@ __global__ __launch_bounds__(256) void rs_route_kernel(RouteArgs p) {
   } else if (p.bias) {
     float b[RUN];
     load_run<RUN>(p.bias, RS_F32, first, held, b);
+    uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < RUN; ++j) {
       if (special) b[j] = j < held ? b[j] : 0.0f;
-      reach = fmaxf(reach, fabsf(b[j]));
+      top = max(top, __float_as_uint(b[j]) & 0x7FFFFFFFu);
       v[j] += b[j];
+    }
+    reach = __uint_as_float(top);
+    if (__ballot(top > 0x7F800000u)) {  // a NaN among them: |bias| is at most |v| + 1
+      reach = 0.0f;
+#pragma unroll
+      for (int j = 0; j < RUN; ++j) {
+        reach = fmaxf(reach, fabsf(v[j]) + 1.0f);
+        v[j] = v[j] == v[j] ? v[j] : -INFINITY;
+      }
     }
     reach = row_max16f(reach);
   }

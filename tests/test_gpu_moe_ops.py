@@ -485,3 +485,22 @@ def test_route_token_does_not_depend_on_its_neighbours(score):
     for t in range(40):
         i, v = run_route(x[t:t + 1], c, bias)
         assert torch.equal(ids[t:t + 1], i) and torch.equal(w[t:t + 1].view(torch.int32), v.view(torch.int32))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,group_top", [(1, 1), (4, 1), (4, 2), (3, 2)])
+def test_route_bias_without_a_number(score, groups, group_top):
+    """An expert whose bias is NaN or -infinity is never chosen and adds
+    nothing to its group."""
+    x = logits_for(40, 48, "f32", 12)
+    bias = torch.randn(48, generator=torch.Generator().manual_seed(1)) * 0.1
+    bias[2::3] = float("nan")
+    if groups == 3:
+        bias[[1, 16, 31]] = -float("inf")
+    plain = torch.where(torch.isnan(bias), torch.full_like(bias, -float("inf")), bias)
+    for k in (4, 14):
+        c = dict(k=k, score=score, renorm=True, groups=groups, top_groups=(groups + 1) // 2, group_top=group_top)
+        ids, w = run_route(x, c, bias.cuda())
+        want, ww, tol = H.route(f64(x), c, f64(plain))
+        assert np.array_equal(ids.cpu().numpy(), want)
+        H.close(f64(w), ww, np.abs(ww) * tol[:, None], "f32", "weights")
