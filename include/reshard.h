@@ -455,7 +455,8 @@ typedef struct rs_fp8_quant {
  * the sign of zero kept.  A block whose scale would be below 2^-126 gets
  * scale 0 and zero codes; a block holding a NaN or an infinity gets a NaN
  * scale and codes 0x7F (as the MXFP8 installation marks such blocks).
- * Float32 products that overflow in a gated value count as infinities.
+ * Float32 products that overflow in a gated value count as infinities; a gate
+ * below -87, whose exp is a subnormal float32, has as many bits as that.
  * row_count (optional; device memory, one int32): only the first *row_count
  * rows of x are quantised, later rows of the outputs are left as they were
  * (reshard_moe_sort's offsets + n_experts; batch 1, block_rows 1, no

@@ -340,3 +340,54 @@ def test_linear_layer_forward_and_both_gradients():
     product(quantise(x), wq, 128, K)
     product(quantise(dy), wt, 128, N)
     product(quantise(dy, transpose=True), quantise(x, transpose=True), 1, M)
+
+
+@pytest.mark.parametrize("block_rows,transpose", [(1, False), (1, True), (128, False), (128, True)])
+def test_quantise_gated_small_sigmoids(block_rows, transpose):
+    """Gates far below 0, whose sigmoid is a subnormal float32: e^gate is off
+    by one of the smallest steps, 2^-149 (its product with the gate by a 70th of
+    that), and the value by the 10 U of any gated one."""
+    rng = np.random.default_rng(2)
+    rows, cols = 150, 260
+    gate = rng.uniform(-101, -70, (rows, cols)).astype(np.float32)
+    gate[:, 128:256] = rng.uniform(-101, -89, (rows, 128))
+    up = (rng.normal(0, 1, (rows, cols)) * 2.0 ** 100).astype(np.float32)
+    x = torch.from_numpy(np.concatenate([gate, up], 1))
+    e = np.exp(gate.astype(np.float64))
+    v = gate * e / (1 + e) * up
+    off = np.abs(v) * (10 * H.U + 1.02 * 2.0 ** -149 / e)
+    v, off = (v.T, off.T) if transpose else (v, off)
+    q, s = run_quantise(x.cuda(), "f32", rows, cols, gated=True, block_rows=block_rows, transpose=transpose)
+    M, K = v.shape
+    for r in range(s.shape[0]):
+        for b in range(s.shape[1]):
+            at = (slice(r * block_rows, (r + 1) * block_rows), slice(b * 128, (b + 1) * 128))
+            want = np.abs(v[at]).max() / 448
+            assert abs(s[r, b] - want) <= off[at].max() / 448 + want * H.U, (r, b, s[r, b], want)
+    sc = H.spread(s, block_rows, M, K)
+    room = np.maximum(np.abs(v) * 2.0 ** -4, sc * 2.0 ** -10) * (1 + 2.0 ** -10) + 2 * off
+    assert (np.abs(H.mxfp8.e4m3_decode(q) * sc - v) <= room).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_quantise_gated_in_square_blocks_and_batches(dtype, transpose):
+    g = torch.Generator().manual_seed(4)
+    n, rows, cols = 3, 200, 150
+    x = (torch.randn(n, rows, 2 * cols, generator=g) * 3).to(DT[dtype])
+    orows, ocols = (cols, rows) if transpose else (rows, cols)
+    q = torch.zeros(n, orows, ocols, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(n, 2, 2, device="cuda")
+    B.reshard_fp8_quantise(B.Fp8Quant(dtype, rows, cols, batch=n, gated=True, block_rows=128, transpose=transpose), ptr(x.cuda()),
+                           None, ptr(q), ptr(s), stream())
+    for i in range(n):
+        gate, up = f64(x[i, :, :cols]), f64(x[i, :, cols:])
+        v = gate / (1 + np.exp(-gate)) * up
+        v = v.T if transpose else v
+        for r in range(2):
+            for b in range(2):
+                want = np.abs(v[r * 128:(r + 1) * 128, b * 128:(b + 1) * 128]).max() / 448
+                assert abs(float(s[i, r, b]) - want) <= want * 11 * H.U
+        sc = H.spread(s[i].cpu().numpy(), 128, orows, ocols)
+        room = np.maximum(np.abs(v) * 2.0 ** -4, sc * 2.0 ** -10) * (1 + 2.0 ** -10) + np.abs(v) * 16 * H.U
+        assert (np.abs(H.mxfp8.e4m3_decode(q[i].cpu().numpy()) * sc - v) <= room).all()
