@@ -391,3 +391,35 @@ def test_quantise_gated_in_square_blocks_and_batches(dtype, transpose):
         sc = H.spread(s[i].cpu().numpy(), 128, orows, ocols)
         room = np.maximum(np.abs(v) * 2.0 ** -4, sc * 2.0 ** -10) * (1 + 2.0 ** -10) + np.abs(v) * 16 * H.U
         assert (np.abs(H.mxfp8.e4m3_decode(q[i].cpu().numpy()) * sc - v) <= room).all()
+
+
+# Streamed rows (few a group), tiles of 64 rows and of 128.
+@pytest.mark.parametrize("M,N,K,G", [(40, 64, 128, 16), (40, 64, 128, 3), (1500, 3000, 256, 3)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_matmul_rows_without_a_group_are_left(M, N, K, G, out):
+    """Rows before the first offset and behind the last, offsets beyond m
+    (cut to it) and below 0, descending ones (an empty group): what a group
+    holds is its product, every other row keeps what it had."""
+    rng = np.random.default_rng(M)
+    a, b = Operand(rng, 1, M, K, 1), Operand(rng, G, N, K, 128)
+    at = lambda *p: [int(v * M) for v in p]
+    for ends in (at(0, .7, 1.2, 2.2), at(.12, .25, .25, .5), at(0, .75, .5, .62), at(-.2, .1, .1, .1), at(1.5, 1.6, 1.7, 1.8),
+                 at(.5, .5, .5, .5), at(.9, .2, .3, 1)):
+        off = np.array([ends[0]] * (G - 3) + ends, dtype=np.int32)
+        c = Guarded(M, N, DT[out])
+        before = c.t.clone()
+        mm = B.Fp8Matmul(M, N, K, out, groups=G, a_stride=a.ld, b_stride=b.ld)
+        B.reshard_fp8_matmul(mm, ptr(a.dev), ptr(a.sdev), None, ptr(b.dev), ptr(b.sdev), ptr(torch.from_numpy(off).cuda()),
+                             c.ptr, stream())
+        torch.cuda.synchronize()
+        cut = np.clip(off, 0, M)
+        held = np.zeros(M, dtype=int)   # groups that name a row: two where offsets descend
+        for g in range(G):
+            held[cut[g]:max(cut[g], cut[g + 1])] += 1
+        for g in range(G):
+            rows = [i for i in range(cut[g], max(cut[g], cut[g + 1])) if held[i] == 1]
+            want, tol = H.product(a.values[0][rows], b.values[g], -(-K // 128), out)
+            H.close(f64(c.t)[rows], want, tol, out, "group %d" % g)
+        left = torch.from_numpy(held == 0).cuda()
+        assert torch.equal(c.t[left].contiguous().view(torch.uint8), before[left].contiguous().view(torch.uint8))
+        assert c.intact()
