@@ -489,18 +489,22 @@ typedef struct rs_fp8_matmul {
 
 /* c[i, n] = sum over blocks kb of 128 columns of
  *   a_scales[r, kb] * b_scales[g, block(n), kb] * sum_{k in kb} a[r, k] * b[g, n, k]
- * summed in float32 and rounded once to c's type.  For a float32 c the inner
- * sums are formed on the bfloat16 matrix path and are exact to float32; for a
- * 16-bit c on the FP8 path, twice as fast, which cuts each product 13 bits
- * below the largest of its eight neighbours (a relative error near 1.3e-5 on
- * normally distributed values, far below the rounding of c).  r = i, or a_index[i] (an
- * index outside [0, a_rows) reads as a row of zeros).  Without groups g = 0
- * and offsets is NULL; with them row i belongs to the group g with
- * offsets[g] <= i < offsets[g + 1] (n_groups + 1 ascending entries on the
- * device, reshard_moe_sort's), and rows of c from offsets[n_groups] on (or
- * before offsets[0]) are left as they were.  a, b: 16-byte aligned, and
- * their rows, the last one too, are memory up to the next multiple of 16
- * bytes behind column k (its contents have no effect). */
+ * summed in float32 and rounded once to c's type.  The product a_scales *
+ * b_scales is formed first, in float32, and has to lie within its range.
+ * For a float32 or f16 c the inner sums are formed on the bfloat16 matrix path
+ * and are exact to float32.  For a bf16 c they are formed on the FP8 path,
+ * twice as fast, which cuts each product 13 bits below the largest of its
+ * eight neighbours: at most 2^-10 of the sum of the products' magnitudes
+ * (measured on normally distributed values 1.4e-5 of the rms result, with one
+ * column in 128 a hundred times the others 5e-5; a small result of large
+ * products that cancel can be off by more than bf16's own 2^-8).
+ * r = i, or a_index[i] (an index outside [0, a_rows) reads as a row of zeros).
+ * Without groups g = 0 and offsets is NULL; with them row i belongs to the
+ * group g with offsets[g] <= i < offsets[g + 1] (n_groups + 1 ascending
+ * entries on the device, reshard_moe_sort's), and rows of c from
+ * offsets[n_groups] on (or before offsets[0]) are left as they were.  a, b:
+ * 16-byte aligned, and their rows, the last one too, are memory up to the next
+ * multiple of 16 bytes behind column k (its contents have no effect). */
 rs_status reshard_fp8_matmul(const rs_fp8_matmul* mm, const uint8_t* a, const float* a_scales,
                              const int32_t* a_index, const uint8_t* b, const float* b_scales,
                              const int32_t* offsets, void* c, void* stream);

@@ -423,3 +423,55 @@ def test_matmul_rows_without_a_group_are_left(M, N, K, G, out):
         left = torch.from_numpy(held == 0).cuda()
         assert torch.equal(c.t[left].contiguous().view(torch.uint8), before[left].contiguous().view(torch.uint8))
         assert c.intact()
+
+
+def outlier_codes(rng, R, K, large, small):
+    """Rows whose every eighth column holds `large`, the others `small` (E4M3 codes)."""
+    q = np.full((R, K), small, dtype=np.uint8)
+    q[:, ::8] = large
+    return q
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 64, 1024), (20, 100, 1040), (40, 200, 1024), (300, 300, 1000), (2900, 3000, 392)])
+@pytest.mark.parametrize("b_rows", [128, 1])
+def test_matmul_f16_keeps_small_products_next_to_large_ones(M, N, K, b_rows):
+    """Large products that cancel: the small ones between them are the result,
+    and float32 sums hold them (448 * 448 + 2 * 2 takes 17 bits)."""
+    rng = np.random.default_rng(0)
+    a, b = Operand(rng, 1, M, K, 1), Operand(rng, 1, N, K, b_rows)
+    top, two = 0x7E, 0x40   # 448 and 2
+    qa, qb = outlier_codes(rng, M, K, top, two), outlier_codes(rng, N, K, top, two)
+    qb[:, 8::16] |= 0x80    # every other large product is negative
+    for o, q in ((a, qa), (b, qb)):
+        o.dev[0, :, :K] = torch.from_numpy(q).cuda()
+        o.sdev.fill_(0.5)
+    want, tol = H.product(H.mxfp8.e4m3_decode(qa) * 0.5, H.mxfp8.e4m3_decode(qb) * 0.5, -(-K // 128), "f32")
+    c = Guarded(M, N, torch.float16)
+    mm = B.Fp8Matmul(M, N, K, "f16", a_stride=a.ld, b_stride=b.ld, b_block_rows=b_rows)
+    B.reshard_fp8_matmul(mm, ptr(a.dev), ptr(a.sdev), None, ptr(b.dev), ptr(b.sdev), None, c.ptr, stream())
+    torch.cuda.synchronize()
+    H.close(f64(c.t), want, tol, "f16", "c")
+    assert c.intact()
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M", [3, 40, 700])
+def test_matmul_outlier_columns(M, out):
+    """Activations with a column in 128 a hundred times the others."""
+    rng = np.random.default_rng(M)
+    N, K = 300, 1024
+    x, w = rng.normal(0, 1, (M, K)), rng.normal(0, 0.02, (N, K))
+    x[:, 5::128] *= 100
+    (qa, sa), (qb, sb) = H.quantise(x, 1), H.quantise(w, 128)
+    want, tol = H.product(H.values(qa, sa, 1), H.values(qb, sb, 128), 8, "f32" if out == "f16" else out)
+    c = Guarded(M, N, DT[out])
+    B.reshard_fp8_matmul(B.Fp8Matmul(M, N, K, out), ptr(torch.from_numpy(qa).cuda()), ptr(torch.from_numpy(sa).cuda()), None,
+                         ptr(torch.from_numpy(qb).cuda()), ptr(torch.from_numpy(sb).cuda()), None, c.ptr, stream())
+    torch.cuda.synchronize()
+    H.close(f64(c.t), want, tol, out, "c")
+
+
+@pytest.mark.parametrize("M,N,K", [(2900, 3000, 392), (1900, 3000, 392), (1000, 3000, 4000)])
+def test_matmul_f16_many_tiles(M, N, K):
+    check_matmul(M, N, K, "f16", c_pad=5, seed=M, factor=2.0 ** -12)
+    check_matmul(0, N, K, "f16", groups=[M // 2, 0, 1, M // 3, 65], index_rows=300, tail=9, seed=K, factor=2.0 ** -12)
