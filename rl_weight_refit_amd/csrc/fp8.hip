@@ -580,6 +580,27 @@ __device__ __forceinline__ void load_lds4(uint32_t to, const void* base, uint32_
       ".Lskip%=:" ::"s"(to), "v"(off), "s"(base), "s"(kb), "s"(end)
       : "memory", "scc");
 }
+// The same from addresses that a 32-bit offset does not reach.
+__device__ __forceinline__ void load_lds16(uint32_t to, const void* base, uint64_t off, int kb, int end) {
+  asm volatile(
+      "s_cmp_ge_i32 %2, %3\n\t"
+      "s_cbranch_scc1 .Lskip%=\n\t"
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, off\n"
+      ".Lskip%=:" ::"s"(to), "v"(reinterpret_cast<uint64_t>(base) + off), "s"(kb), "s"(end)
+      : "memory", "scc");
+}
+__device__ __forceinline__ void load_lds4(uint32_t to, const void* base, uint64_t off, int kb, int end) {
+  asm volatile(
+      "s_cmp_ge_i32 %2, %3\n\t"
+      "s_cbranch_scc1 .Lskip%=\n\t"
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %1, off\n"
+      ".Lskip%=:" ::"s"(to), "v"(reinterpret_cast<uint64_t>(base) + off), "s"(kb), "s"(end)
+      : "memory", "scc");
+}
 // Waits until at most N of this wave's loads are under way.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -634,8 +655,10 @@ __device__ __forceinline__ bool tile_of(uint32_t id, uint32_t row_tiles, uint32_
   return true;
 }
 
-template <int BM, int BN, int WM, int S, int KG, bool EACH, bool EXACT>
+// FAR: load offsets of 64 bits.
+template <int BM, int BN, int WM, int S, int KG, bool EACH, bool EXACT, bool FAR = false>
 struct Tile {
+  using Offset = std::conditional_t<FAR, uint64_t, uint32_t>;
   // Two stages: the two waves of a SIMD (w and w + 4) take turns at reading
   // LDS and multiplying; see the loops.
   static constexpr bool kTurns = S == 2 && KG == 1 && !EXACT;
@@ -647,10 +670,10 @@ struct Tile {
 
 // Rows [begin, end) of group g, columns from n0.  absent[r]: gathered row r lies
 // outside a.
-template <int BM, int BN, int WM, int S, int KG, bool EACH, bool EXACT>
-__device__ __forceinline__ void Tile<BM, BN, WM, S, KG, EACH, EXACT>::run(const MatmulArgs& p, uint8_t* lds,
-                                                                          uint8_t* absent, int g, int64_t begin,
-                                                                          int64_t end, int n0) {
+template <int BM, int BN, int WM, int S, int KG, bool EACH, bool EXACT, bool FAR>
+__device__ __forceinline__ void Tile<BM, BN, WM, S, KG, EACH, EXACT, FAR>::run(const MatmulArgs& p, uint8_t* lds,
+                                                                               uint8_t* absent, int g, int64_t begin,
+                                                                               int64_t end, int n0) {
   constexpr int WN = 8 / WM / KG, MT = BM / WM / 16, NT = BN / WN / 16;   // 16 x 16 tiles per wave: MT x NT
   constexpr int LA = BM / 64, LB = BN / 64;                          // 16-byte loads per lane and stage
   static_assert(!kTurns || (WN * 128 == BN && NT == 8), "a wave's first four column tiles lie in b's even pieces");
@@ -664,25 +687,25 @@ __device__ __forceinline__ void Tile<BM, BN, WM, S, KG, EACH, EXACT>::run(const 
   // from the last, gathered rows outside a from row 0; neither is stored.
   const auto a_row = [&](int r) {
     const int64_t i = min(begin + r, end - 1);
-    if (!p.index) return uint32_t(i - begin);
+    if (!p.index) return Offset(i - begin);
     const int64_t at = p.index[i];
-    return uint32_t(at >= 0 && at < p.a_rows ? at : 0);
+    return Offset(at >= 0 && at < p.a_rows ? at : 0);
   };
   if (p.index && tid < BM) {
     const int64_t at = p.index[min(begin + tid, end - 1)];
     absent[tid] = at < 0 || at >= p.a_rows;
   }
   const int chunk = (lane & 7) ^ (lane >> 3);
-  uint32_t aoff[LA], boff[LB], soff = 0;
+  Offset aoff[LA], boff[LB], soff = 0;
 #pragma unroll
-  for (int i = 0; i < LA; ++i) aoff[i] = a_row(i * 64 + wave * 8 + (lane >> 3)) * uint32_t(p.lda) + chunk * 16;
+  for (int i = 0; i < LA; ++i) aoff[i] = a_row(i * 64 + wave * 8 + (lane >> 3)) * Offset(p.lda) + chunk * 16;
 #pragma unroll
-  for (int i = 0; i < LB; ++i) boff[i] = uint32_t(min(i * 64 + wave * 8 + (lane >> 3), p.n - 1 - n0)) * uint32_t(p.ldb) + chunk * 16;
+  for (int i = 0; i < LB; ++i) boff[i] = Offset(min(i * 64 + wave * 8 + (lane >> 3), p.n - 1 - n0)) * Offset(p.ldb) + chunk * 16;
   const bool sa_wave = wave < LA, sb_wave = wave >= 4 && wave < 4 + (EACH ? LB : 1);
   static_assert(LA <= 4 && LB <= 4, "one wave's load per 64 scales");
   const int scale_end = __builtin_amdgcn_readfirstlane(sa_wave || sb_wave ? INT32_MAX : 0);
-  if (sa_wave) soff = a_row(wave * 64 + lane) * uint32_t(p.ldsa) * 4;
-  else if (sb_wave) soff = uint32_t(b_block(p, min(n0 + (EACH ? (wave - 4) * 64 + lane : (lane & 1) * 128), p.n - 1))) * uint32_t(p.ldsb) * 4;
+  if (sa_wave) soff = a_row(wave * 64 + lane) * Offset(p.ldsa) * 4;
+  else if (sb_wave) soff = Offset(b_block(p, min(n0 + (EACH ? (wave - 4) * 64 + lane : (lane & 1) * 128), p.n - 1))) * Offset(p.ldsb) * 4;
 
   const uint32_t lds0 = lds_address(lds);
   // The loads of block kb < to_kb, in two parts: a, b's even 64-row pieces and
@@ -982,9 +1005,9 @@ __device__ __forceinline__ void Tile<BM, BN, WM, S, KG, EACH, EXACT>::run(const 
 
 // A group's last tile has half its rows or fewer in half of the cases: then it
 // goes as one of half the height, which takes two thirds of the time.
-template <int BM, int BN, int WM, int S, int KG, bool EACH, bool EXACT>
-__global__ __launch_bounds__(512, BM * BN > 128 * 128 || KG > 1 ? 2 : 4) void rs_matmul_tile_kernel(MatmulArgs p, uint32_t row_tiles) {
-  using Whole = Tile<BM, BN, WM, S, KG, EACH, EXACT>;
+template <int BM, int BN, int WM, int S, int KG, bool EACH, bool EXACT, bool FAR>
+__global__ __launch_bounds__(512, BM * BN > 128 * 128 || KG > 1 || FAR ? 2 : 4) void rs_matmul_tile_kernel(MatmulArgs p, uint32_t row_tiles) {
+  using Whole = Tile<BM, BN, WM, S, KG, EACH, EXACT, FAR>;
   using Half = Tile<128, 256, 2, 3, 1, EACH, EXACT>;
   constexpr bool kHalves = BM == 256;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kHalves && Half::kLds > Whole::kLds ? Half::kLds : Whole::kLds];
@@ -1008,16 +1031,16 @@ __global__ __launch_bounds__(512, BM * BN > 128 * 128 || KG > 1 ? 2 : 4) void rs
 // A launch holds fewer than 2^32 threads.
 inline bool too_many(int64_t workgroups, int64_t threads) { return workgroups * threads > int64_t(UINT32_MAX); }
 
-template <int BM, int BN, int WM, int S, int KG>
+template <int BM, int BN, int WM, int S, int KG, bool FAR = false>
 hipError_t launch_tile(MatmulArgs p, bool each, bool exact, int64_t row_tiles, hipStream_t stream) {
   p.n_tiles = (p.n + BN - 1) / BN;
   if (too_many(row_tiles * p.n_tiles, 512)) return hipErrorInvalidConfiguration;
   const uint32_t tiles = uint32_t(row_tiles);
   const dim3 grid(tiles * p.n_tiles);
-  if (each && exact) rs_matmul_tile_kernel<BM, BN, WM, S, KG, true, true><<<grid, 512, 0, stream>>>(p, tiles);
-  else if (each) rs_matmul_tile_kernel<BM, BN, WM, S, KG, true, false><<<grid, 512, 0, stream>>>(p, tiles);
-  else if (exact) rs_matmul_tile_kernel<BM, BN, WM, S, KG, false, true><<<grid, 512, 0, stream>>>(p, tiles);
-  else rs_matmul_tile_kernel<BM, BN, WM, S, KG, false, false><<<grid, 512, 0, stream>>>(p, tiles);
+  if (each && exact) rs_matmul_tile_kernel<BM, BN, WM, S, KG, true, true, FAR><<<grid, 512, 0, stream>>>(p, tiles);
+  else if (each) rs_matmul_tile_kernel<BM, BN, WM, S, KG, true, false, FAR><<<grid, 512, 0, stream>>>(p, tiles);
+  else if (exact) rs_matmul_tile_kernel<BM, BN, WM, S, KG, false, true, FAR><<<grid, 512, 0, stream>>>(p, tiles);
+  else rs_matmul_tile_kernel<BM, BN, WM, S, KG, false, false, FAR><<<grid, 512, 0, stream>>>(p, tiles);
   return hipGetLastError();
 }
 
@@ -1062,28 +1085,33 @@ hipError_t launch_matmul(const rs_fp8_matmul& mm, const uint8_t* a, const float*
                int32_t(mm.n), int32_t(mm.k), mm.n_groups, int32_t(blocks128(mm.k)), 0,
                int32_t(mm.b_split ? mm.b_split : mm.n), int32_t(blocks128(mm.b_split)), mm.out_dtype, mm.b_block_rows};
   const bool each = mm.b_block_rows == 1 || mm.b_split % kBlock != 0, exact = mm.out_dtype != RS_BF16;
-  const int64_t kFar = int64_t(1) << 32;  // the large tiles' load offsets are 32 bits, from a tile's first row or from a
+  const int64_t kFar = int64_t(1) << 32;  // the tiles' load offsets are 32 bits, from a tile's first row or from a
   const int64_t reach = a_index ? mm.a_rows : 256;
-  const bool near = mm.a_rows > 0 && reach * mm.a_stride < kFar && reach * mm.a_scale_stride * 4 < kFar &&
-                    256 * mm.b_stride < kFar && (mm.n + 256) * mm.b_scale_stride * 4 < kFar;
+  const bool near = reach * mm.a_stride < kFar && reach * mm.a_scale_stride * 4 < kFar && 256 * mm.b_stride < kFar &&
+                    (mm.n + 256) * mm.b_scale_stride * 4 < kFar;
   const auto row_tiles = [&](int64_t rows) {
     return mm.m / rows + (mm.n_groups ? min(int64_t(mm.n_groups), mm.m) : (mm.m % rows != 0));
   };
   const int64_t rows = mm.m / (mm.n_groups ? mm.n_groups : 1);  // a group's, on average
-  if (!near || p.kblocks == 0 || rows <= (mm.n_groups ? 4 : 32)) {
-    // Few rows: b streams through registers.  (So do operands too far apart for
-    // the tiles' 32-bit offsets.)  Measured (us, this choice against the
-    // nearest other): 32 experts of 4096 x 7168, two rows each, 133 with 16 x
-    // 64 per workgroup, 136 with 32 x 64; 32 of 2816 x 621, two rows each, 14.7
-    // with 16 x 64, 16.2 with tiles of 64 x 128; but five rows each over 64
-    // experts of 2048 x 1024 24 with tiles, 27 with 16 x 64, and sixteen of 4096
-    // x 7168 167 with tiles, 183 with 32 x 64.  One product 7168 x 4096: one row
-    // 9.0 with 16 x 16, 10.5 with 16 x 32; 20 rows 11.6 with 32 x 32, 13.2 with
-    // tiles of 64 x 64; but 33 rows 13.3 with tiles, 17 with 32 x 64.
+  if (mm.a_rows == 0 || p.kblocks == 0 || rows <= (mm.n_groups ? 4 : 32)) {
+    // Few rows (or nothing to add up): b streams through registers.  Measured
+    // (us, this choice against the nearest other): 32 experts of 4096 x 7168,
+    // two rows each, 133 with 16 x 64 per workgroup, 136 with 32 x 64; 32 of 2816
+    // x 621, two rows each, 14.7 with 16 x 64, 16.2 with tiles of 64 x 128; but
+    // five rows each over 64 experts of 2048 x 1024 24 with tiles, 27 with 16 x
+    // 64, and sixteen of 4096 x 7168 167 with tiles, 183 with 32 x 64.  One
+    // product 7168 x 4096: one row 9.0 with 16 x 16, 10.5 with 16 x 32; 20 rows
+    // 11.6 with 32 x 32, 13.2 with tiles of 64 x 64; but 33 rows 13.3 with tiles,
+    // 17 with 32 x 64.
     if (mm.n_groups && rows <= 4) return launch_stream<1, 4, 2, 4>(p, each, exact, row_tiles(16), stream);
     if (!mm.n_groups && rows <= 16) return launch_stream<1, 1, 4, 8>(p, each, exact, row_tiles(16), stream);
     return launch_stream<2, 2, 2, 8>(p, each, exact, row_tiles(32), stream);
   }
+  // Operands too far apart for offsets of 32 bits: one shape with 64-bit ones,
+  // which has the registers for them.  Measured (us): 8192 rows gathered from 4.3
+  // GB over 32 experts of 7168 x 2048 278, streamed 921 (from 4.1 GB, 32 bits:
+  // 211); 16,384 x 4096 x 7168 772, streamed 3,566 (32 bits: 388).
+  if (!near) return launch_tile<64, 256, 1, 3, 1, true>(p, each, exact, row_tiles(64), stream);
   // The tile shape with the least expected time: rounds of workgroups over
   // the chip, each of a fixed time and a time per step, fitted to measured
   // times (us): with every compute unit busy, or with one workgroup a unit

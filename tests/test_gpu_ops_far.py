@@ -108,3 +108,70 @@ def test_route_far_rows():
         B.reshard_moe_route_grad(r, T, ptr(t), stride, ptr(ids), ptr(w), ptr(out), stride, stream())
         got.append((ids.cpu(), w.cpu(), out.contiguous().cpu()))
     assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(*got))
+
+
+# What the tiles' 32-bit offsets do not reach: gathered rows spread over 4 GiB or more, and rows of either side (or their
+# scales) so far apart that one tile's span as much.
+@pytest.mark.parametrize("side,rows,stride", [("a gathered", 4200, 1 << 20), ("a gathered", 9000, 1 << 19), ("a", 150, 1 << 25),
+                                              ("b", 150, 1 << 25), ("a scales", 150, 1 << 23), ("b scales", 330, 1 << 22)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_matmul_tiles_beyond_32_bit_offsets(side, rows, stride, out):
+    rng = np.random.default_rng(rows)
+    M, N, K = (rows, 300, 408) if side[0] == "a" else (320, rows, 408)
+    codes = [torch.from_numpy(H.random_codes(rng, r, 416)) for r in (M, N)]
+    scales = [torch.from_numpy(rng.uniform(0.5, 2.0, (r, 4)).astype(np.float32)) for r in (M, N)]
+    values = [H.mxfp8.e4m3_decode(c.numpy()) * np.repeat(f64(s), 128, 1)[:, :416] for c, s in zip(codes, scales)]
+    a, b = (placed(t, stride) if name in (side, side[:-9]) else t.cuda() for t, name in zip(codes, "ab"))
+    sa, sb = (placed(t, stride) if name + " scales" == side else t.cuda() for t, name in zip(scales, "ab"))
+    order = rng.integers(-1, M + 1, 700).astype(np.int32) if side == "a gathered" else np.arange(M, dtype=np.int32)
+    order[:2] = [M - 1, 0]
+    idx = torch.from_numpy(order).cuda() if side == "a gathered" else None
+    if idx is None:
+        order = np.arange(M)
+    c = torch.zeros(len(order), N, dtype=H.DT[out], device="cuda")
+    mm = B.Fp8Matmul(len(order), N, K, out, a_rows=M, a_stride=a.stride(0), a_scale_stride=sa.stride(0), b_stride=b.stride(0),
+                     b_scale_stride=sb.stride(0), b_block_rows=1)
+    B.reshard_fp8_matmul(mm, ptr(a), ptr(sa), ptr(idx), ptr(b), ptr(sb), None, ptr(c), stream())
+    av = np.where(((order >= 0) & (order < M))[:, None], values[0][np.clip(order, 0, M - 1)], 0.0)
+    want, tol = H.product(av[:, :K], values[1][:, :K], 4, out)
+    H.close(f64(c), want, tol, out, "c")
+
+
+def test_matmul_far_gathered_groups():
+    rng = np.random.default_rng(3)
+    M, N, K, rows = 300, 256, 256, 4200
+    a, sa = torch.from_numpy(H.random_codes(rng, rows, K)), rng.uniform(0.5, 2.0, (rows, 2)).astype(np.float32)
+    b, sb = torch.from_numpy(H.random_codes(rng, 2 * N, K)), rng.uniform(0.5, 2.0, (2, 2, 2)).astype(np.float32)
+    far_a = placed(a, 1 << 20)
+    far_b = torch.empty((1 << 32) + N * K, dtype=torch.uint8, device="cuda").as_strided((2, N, K), (1 << 32, K, 1))
+    far_b.copy_(b.view(2, N, K))
+    off, idx = np.array([0, 170, 300], dtype=np.int32), rng.integers(0, rows, M).astype(np.int32)
+    c = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    mm = B.Fp8Matmul(M, N, K, "bf16", groups=2, a_rows=rows, a_stride=1 << 20, b_group_stride=1 << 32)
+    dev = [torch.from_numpy(v).cuda() for v in (sa, idx, sb, off)]
+    B.reshard_fp8_matmul(mm, ptr(far_a), ptr(dev[0]), ptr(dev[1]), ptr(far_b), ptr(dev[2]), ptr(dev[3]), ptr(c), stream())
+    av = (H.mxfp8.e4m3_decode(a.numpy()) * np.repeat(sa.astype(np.float64), 128, 1))[idx]
+    bv = H.mxfp8.e4m3_decode(b.numpy()).reshape(2, N, K) * np.repeat(np.repeat(sb.astype(np.float64), 128, 1), 128, 2)
+    for g in range(2):
+        want, tol = H.product(av[off[g]:off[g + 1]], bv[g], 2, "bf16")
+        H.close(f64(c[off[g]:off[g + 1]]), want, tol, "bf16", "group %d" % g)
+
+
+def test_matmul_far_gathered_rows_in_one_launch():
+    """2.2 million rows gathered from 4 GiB, by 4096 columns: 550,000 tiles of
+    64 x 256, where one of 32 x 32 each would take more threads than a launch
+    holds."""
+    rng = np.random.default_rng(4)
+    M, N, K, rows = 2_200_000, 4096, 128, 4200
+    a, sa = torch.from_numpy(H.random_codes(rng, rows, K)), rng.uniform(0.5, 2.0, (rows, 1)).astype(np.float32)
+    b, sb = torch.from_numpy(H.random_codes(rng, N, K)), rng.uniform(0.5, 2.0, (N // 128, 1)).astype(np.float32)
+    idx = rng.integers(0, rows, M).astype(np.int32)
+    far_a, c = placed(a, 1 << 20), torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    dev = [torch.from_numpy(v).cuda() for v in (sa, idx, sb)]
+    bd = b.cuda()
+    mm = B.Fp8Matmul(M, N, K, "bf16", a_rows=rows, a_stride=1 << 20)
+    B.reshard_fp8_matmul(mm, ptr(far_a), ptr(dev[0]), ptr(dev[1]), ptr(bd), ptr(dev[2]), None, ptr(c), stream())
+    some = np.concatenate([np.arange(70), np.arange(M - 70, M), rng.integers(0, M, 400)])
+    av = (H.mxfp8.e4m3_decode(a.numpy()) * sa.astype(np.float64))[idx[some]]
+    want, tol = H.product(av, H.mxfp8.e4m3_decode(b.numpy()) * np.repeat(sb.astype(np.float64), 128, 0), 1, "bf16")
+    H.close(f64(c[torch.from_numpy(some).cuda()]), want, tol, "bf16", "c")
