@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import matmul_shapes
 import ops_helpers as H
 from ops_helpers import B, DT, Guarded, f64, ptr, stream, strided
 
@@ -475,3 +476,14 @@ def test_matmul_outlier_columns(M, out):
 def test_matmul_f16_many_tiles(M, N, K):
     check_matmul(M, N, K, "f16", c_pad=5, seed=M, factor=2.0 ** -12)
     check_matmul(0, N, K, "f16", groups=[M // 2, 0, 1, M // 3, 65], index_rows=300, tail=9, seed=K, factor=2.0 ** -12)
+
+
+@pytest.mark.parametrize("b_rows", [128, 1])
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("case", range(len(matmul_shapes.CASES)))
+def test_matmul_every_kernel(case, out, b_rows):
+    """Each kernel's forms: plain and gathered rows, every result, both scale forms."""
+    _, groups, M, N, K = matmul_shapes.CASES[case]
+    factor = 2.0 ** -12 if out == "f16" else 1.0   # f16 results that do not overflow
+    check_matmul(M, N, K, out, groups=groups, b_rows=b_rows, c_pad=3, seed=case, factor=factor)
+    check_matmul(M, N, K, out, groups=groups, b_rows=b_rows, index_rows=300, seed=case, factor=factor)
