@@ -413,7 +413,11 @@ rs_status reshard_moe_route(const rs_router* router, int64_t n_tokens, const voi
  * instance those of the generation side, replayed): each slot counts by
  * itself, also where two name the same expert; an id outside [0, n_experts)
  * is an empty slot.  The same formulas as the forward pass hold, over the
- * slots given: NaN and -infinity logits have score and gradient 0. */
+ * slots given: NaN and -infinity logits have score and gradient 0, and
+ * dweights of slots that name them, or no expert, is not used.  Gradients are
+ * good to float32's rounding of their own magnitude; for softmax weights that
+ * are not renormalised, whose formula is s_e * (dweights_e - sum of dweights *
+ * s), to the rounding of s_e times the largest dweights. */
 rs_status reshard_moe_route_grad(const rs_router* router, int64_t n_tokens, const void* logits,
                                  int64_t logits_stride, const int32_t* ids, const float* dweights,
                                  void* dlogits, int64_t dlogits_stride, void* stream);

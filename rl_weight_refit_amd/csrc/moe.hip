@@ -575,7 +575,8 @@ __global__ __launch_bounds__(RUN > 16 ? 64 : 256) void rs_route_grad_kernel(Rout
     if (id[a] < 0 || id[a] >= p.n_experts) id[a] = -1;
     l[a] = id[a] < 0 ? -INFINITY : load1(p.logits, p.dtype, row + id[a]);
     l[a] = l[a] == l[a] ? l[a] : -INFINITY;
-    h[a] = id[a] < 0 ? 0.0f : p.scale * p.dweights[t * p.top_k + i];
+    // a score that is 0 for good takes no gradient, whatever dweights holds there
+    h[a] = l[a] > -INFINITY ? p.scale * p.dweights[t * p.top_k + i] : 0.0f;
   }
   float mean = 0.0f;
   if (p.renormalise) {

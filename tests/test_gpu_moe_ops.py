@@ -504,3 +504,21 @@ def test_route_bias_without_a_number(score, groups, group_top):
         want, ww, tol = H.route(f64(x), c, f64(plain))
         assert np.array_equal(ids.cpu().numpy(), want)
         H.close(f64(w), ww, np.abs(ww) * tol[:, None], "f32", "weights")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_grad_ignores_dweights_of_slots_without_a_score(score, renorm):
+    x = logits_for(6, 32, "f32", 2)
+    x[:, 5], x[:, 6] = -float("inf"), float("nan")
+    ids = np.tile(np.array([[5, 1, 6, 2, -1, 32]], dtype=np.int32), (6, 1))
+    dw = np.random.default_rng(0).normal(0, 1, (6, 6)).astype(np.float32)
+    clean = dw.copy()
+    clean[:, [0, 2, 4, 5]] = 0.0
+    dw[:3, [0, 2, 4, 5]] = np.nan
+    dw[3:, [0, 2, 4, 5]] = np.inf
+    out = torch.full((6, 32), 7.0, device="cuda")
+    B.reshard_moe_route_grad(B.Router("f32", 32, 6, score=score, renormalise=renorm), 6, ptr(x), 32, ptr(torch.from_numpy(ids).cuda()),
+                             ptr(torch.from_numpy(dw).cuda()), ptr(out), 32, stream())
+    want, tol = H.route_grad(f64(x), ids, clean.astype(np.float64), dict(score=score, renorm=renorm))
+    H.close(f64(out), want, tol, "f32", "dlogits")
