@@ -175,3 +175,72 @@ def test_matmul_far_gathered_rows_in_one_launch():
     av = (H.mxfp8.e4m3_decode(a.numpy()) * sa.astype(np.float64))[idx[some]]
     want, tol = H.product(av, H.mxfp8.e4m3_decode(b.numpy()) * np.repeat(sb.astype(np.float64), 128, 0), 1, "bf16")
     H.close(f64(c[torch.from_numpy(some).cuda()]), want, tol, "bf16", "c")
+
+
+def test_sort_of_the_most_slots():
+    """2^30 slots, against a stable sort."""
+    T, k, E, first, local = 1 << 27, 8, 40, 5, 30
+    ids = torch.randint(-1, E, (T, k), dtype=torch.int32, device="cuda", generator=torch.Generator(device="cuda").manual_seed(0))
+    off = torch.empty(local + 1, dtype=torch.int32, device="cuda")
+    tok, pos = torch.empty(T * k, dtype=torch.int32, device="cuda"), torch.empty(T, k, dtype=torch.int32, device="cuda")
+    ws = torch.empty(B.reshard_moe_sort_workspace(T, k, local), dtype=torch.uint8, device="cuda")
+    B.reshard_moe_sort(ptr(ids), T, k, first, local, ptr(off), ptr(tok), ptr(pos), ptr(ws), ws.numel(), stream())
+    e = ids.view(-1) - first
+    e = torch.where((e >= 0) & (e < local), e, local)
+    counts = torch.bincount(e, minlength=local + 1)
+    want = torch.zeros(local + 1, dtype=torch.int64, device="cuda")
+    want[1:] = counts[:local].cumsum(0)
+    assert torch.equal(off.long(), want)
+    rows = int(want[-1])
+    order = torch.sort(e.to(torch.uint8), stable=True).indices[:rows]
+    assert torch.equal(pos.view(-1)[order], torch.arange(rows, dtype=torch.int32, device="cuda"))
+    assert torch.equal(tok[:rows], torch.div(order, k, rounding_mode="floor").int()) and bool((tok[rows:] == -1).all())
+    assert int((pos == -1).sum()) == T * k - rows
+
+
+def test_quantise_a_row_of_the_most_columns():
+    """One row of 2^31 values has the codes of 2^24 rows of 128."""
+    n = 1 << 31
+    x = torch.randn(1 << 20, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(0)).bfloat16().repeat(16, 1)
+    x[-1] *= 7
+    got = []
+    for rows, cols in ((1, n), (n // 128, 128)):
+        q, s = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty(n // 128, device="cuda")
+        B.reshard_fp8_quantise(B.Fp8Quant("bf16", rows, cols), ptr(x), None, ptr(q), ptr(s), stream())
+        got.append((q, s))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    want = H.quantise(x[-300:].float().cpu().numpy(), 1)
+    assert np.array_equal(got[0][0][-300 * 128:].cpu().numpy(), want[0].reshape(-1)) and np.array_equal(got[0][1][-300:].cpu().numpy(), want[1][:, 0])
+
+
+def test_combine_wide_rows():
+    """Rows of more than 65,535 workgroups of 2048 columns."""
+    n = (1 << 27) + (1 << 24) + 5
+    g = torch.Generator(device="cuda").manual_seed(0)
+    y = torch.randn(3, n, device="cuda", generator=g).bfloat16()
+    pos, w = torch.tensor([[2, 0], [-1, 1]], dtype=torch.int32, device="cuda"), torch.tensor([[0.5, 3.0], [1.0, -0.75]], device="cuda")
+    out = torch.empty(2, n, dtype=torch.bfloat16, device="cuda")
+    B.reshard_moe_combine(B.MoeCombine("bf16", "bf16", 2, 2, n, 3), ptr(y), ptr(pos), ptr(w), ptr(out), stream())
+    # half, -3/4 and thrice of a bf16 value are exact in float32, and so is one rounding of their sum in float64
+    assert torch.equal(out[1], (y[1].float() * -0.75).bfloat16())
+    want = y[2].double() * 0.5 + y[0].double() * 3.0
+    assert bool(((out[0].double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -24) + 1e-38).all())
+
+
+def test_route_of_many_tokens():
+    """Row offsets beyond 2^31 elements."""
+    T, E = (1 << 25) + 3, 72
+    x = torch.randn(1 << 16, E, device="cuda", generator=torch.Generator(device="cuda").manual_seed(0)).bfloat16()
+    whole = torch.empty(T, E, dtype=torch.bfloat16, device="cuda")
+    whole[: 1 << 25].view(512, 1 << 16, E).copy_(x)
+    whole[1 << 25:] = x[:3]
+    r = B.Router("bf16", E, 3, score="sigmoid")
+    got = []
+    for t in (whole, x):
+        ids, w = torch.empty(t.shape[0], 3, dtype=torch.int32, device="cuda"), torch.empty(t.shape[0], 3, device="cuda")
+        B.reshard_moe_route(r, t.shape[0], ptr(t), E, None, None, ptr(ids), ptr(w), stream())
+        dl = torch.empty_like(t)
+        B.reshard_moe_route_grad(r, t.shape[0], ptr(t), E, ptr(ids), ptr(w), ptr(dl), E, stream())
+        got.append((ids, w, dl))
+    for a, b in zip(*got):
+        assert torch.equal(a[: 1 << 25].view(512, 1 << 16, -1), b.expand(512, -1, -1)) and torch.equal(a[1 << 25:], b[:3])
