@@ -200,17 +200,22 @@ __device__ __forceinline__ float value_of(uint32_t k) {
   return __uint_as_float(k ^ (uint32_t(int32_t(~k) >> 31) | 0x80000000u));
 }
 
-// How far the float32 value v = s + bias may be from the exact one.
-// Softmax, with d the logit's distance from the largest: exp(-d) is off by
-// 2 d + 2 units of 2^-24 (the argument rounded twice, one unit of the
-// instruction), the sum by 28 (its terms, weighted, and a tree of additions),
-// quotient and reciprocal by 4, and d is at most -log s: below
-// s (17 - log s) 2^-23.  Sigmoid: exp as before, but only s (1 - s) of it
-// arrives, below 0.8 units; the addition and the reciprocal (one unit of the
-// instruction, 2^-23) leave below 2^-23 (0.4 + 1.5 s).  And v's own rounding.
+// How far the float32 value v = s + bias may be from the exact one, in units
+// of 2^-24.  Softmax, with d the logit's distance from the largest: exp(-d) is
+// off by 2.3 d + 2 (the difference and its product with log2 e rounded, that
+// constant's own error, one step of the instruction), the sum by 11 from its
+// terms (their errors weighted by themselves, of 1024 at the most), by RUN - 1
+// from a lane's additions, each of which may round the same way, and by 4 from
+// the lanes', quotient and product by 2, and d is at most -log s: below
+// s (RUN + 18 + 2.3 (-log s)).  Sigmoid: exp as before, but only s (1 - s) of it
+// arrives, below 0.8; the addition and the reciprocal (one step of the
+// instruction) leave below 0.8 + 3 s.  And v's own rounding; what the
+// instruction makes 0 lies below 2^-126.
+template <int RUN>
 __device__ __forceinline__ float error_of(float s, float v, bool sigmoid) {
-  const float f = sigmoid ? 0.5f + 1.5f * s : s * (17.0f - __logf(s + 1e-30f));
-  return 0x1p-23f * (f + fabsf(v));
+  constexpr float kSum = RUN <= 16 ? 17.0f : (RUN + 18) * 0.5f;
+  const float f = sigmoid ? 0.5f + 1.5f * s : s * (kSum - 1.2f * __logf(s + 0x1p-126f));
+  return fmaf(0x1p-23f, f + fabsf(v), 0x1p-125f);
 }
 
 // The sigmoid and what is left of it to 1, both to a few units of themselves.
@@ -341,7 +346,7 @@ __global__ __launch_bounds__(256) void rs_route_kernel(RouteArgs p) {
     on = before < p.top_groups;
     if (!p.by_logit) {
       // the scores lie within what v and the largest |bias| allow; the error grows with them
-      const auto off = [&](float v) { return error_of(fminf(1.0f, fabsf(v) + reach), v, p.sigmoid); };
+      const auto off = [&](float v) { return error_of<RUN>(fminf(1.0f, fabsf(v) + reach), v, p.sigmoid); };
       const float err = gs > -INFINITY ? off(a) + (two ? off(b) : 0.0f) + 0x1p-23f * fabsf(gs) : 0.0f;
       const float low = row_max16f(on || group >= p.n_groups ? -INFINITY : gs + err);        // the best group left out
       const float high = -row_max16f(on && group < p.n_groups ? err - gs : -INFINITY);       // the last one kept
@@ -398,11 +403,11 @@ __global__ __launch_bounds__(256) void rs_route_kernel(RouteArgs p) {
   // the float32 one by less than RUN steps), and the least.
   const auto most = [&](uint32_t k, float score) {
     const float v = value_of(k | kPlace);
-    return !k ? -INFINITY : p.by_logit ? v : v + error_of(score, v, p.sigmoid);
+    return !k ? -INFINITY : p.by_logit ? v : v + error_of<RUN>(score, v, p.sigmoid);
   };
   const auto least = [&](uint32_t k, float score) {
     const float v = value_of(k & ~kPlace);
-    return p.by_logit ? v : v - error_of(score, v, p.sigmoid);
+    return p.by_logit ? v : v - error_of<RUN>(score, v, p.sigmoid);
   };
 #pragma unroll
   for (int h = 0; h < 3; ++h)

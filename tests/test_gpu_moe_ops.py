@@ -522,3 +522,21 @@ def test_route_grad_ignores_dweights_of_slots_without_a_score(score, renorm):
                              ptr(torch.from_numpy(dw).cuda()), ptr(out), 32, stream())
     want, tol = H.route_grad(f64(x), ids, clean.astype(np.float64), dict(score=score, renorm=renorm))
     H.close(f64(out), want, tol, "f32", "dlogits")
+
+
+@pytest.mark.parametrize("E,G", [(512, 1), (1000, 1), (1024, 1), (1017, 9), (1020, 5)])
+def test_route_where_the_sum_of_exponentials_rounds_one_way(E, G):
+    """Many terms just above half a step of their sum: each addition rounds up,
+    and the largest score comes out low by nearly as many steps.  Next to it
+    stands an expert whose bias alone lies that near."""
+    run = -(-E // 16) if G == 1 else E // G if G > 8 else -(-(E // G) // 2)   # experts a lane
+    x = torch.full((10, E), -100.0)
+    x[:, 0] = 0.0
+    x[:, 1:run] = float(np.log(0.51 * 2.0 ** -23))
+    s = 1 / (1 + np.exp(f64(x[0, 1:run])).sum())
+    other = E // G - 1 if G > 1 else E - 1   # of the same group
+    for gap in (-30, -2, 2, 10, 25, 40, 55, 100):
+        bias = -10.0 - torch.arange(E) * 0.01
+        bias[0] = -0.99
+        bias[other] = float(np.float32(s + float(bias[0]) - gap * H.U))
+        check_route(x.cuda(), dict(k=2, score="softmax", renorm=False, groups=G, top_groups=1), bias.cuda())
