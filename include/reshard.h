@@ -339,8 +339,10 @@ const char* reshard_last_error(void);
  * are put in expert order, activations are quantised with one scale per
  * token and 128 columns, multiplied with the experts' weights on the matrix
  * cores, and the experts' rows combined into the tokens'; with the backward
- * passes of routing and combination, and the quantised forms that the
- * product's own two backward products take.
+ * passes of routing and combination, and the quantised forms that a product's
+ * own backward products take: the input gradient of any, the weight gradient of
+ * one without groups.  (The weight gradients of groups, and the backward pass
+ * of the gated activation, have no call.)
  *
  * Common rules.  Every call enqueues kernels on `stream` (a hipStream_t;
  * NULL = the default stream of the current device) and returns; the kernels

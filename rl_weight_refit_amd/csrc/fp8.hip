@@ -541,8 +541,8 @@ __device__ __forceinline__ uint64_t pack4(f32x4 v) {
 // that a quarter wave reads one chunk of lie in all banks (8192 x 8192 x 8192:
 // 1.6e6 conflict cycles, 4.6e7 in the plain order).
 //
-// 8192 x 8192 x 8192: 490 us, 2,240 TFLOP/s (float32 c, by the bfloat16 path:
-// 880 us).  A copy of the kernel without its loads takes 437 us, one that
+// 8192 x 8192 x 8192: 490 us, 2,240 TFLOP/s (f16 or float32 c, by the bfloat16
+// path: 880 to 890 us).  A copy of the kernel without its loads takes 437 us, one that
 // does not scale either 344 to 360: matrix instructions with the LDS reads that
 // feed them bound it, scaling (four vector FMAs a matrix instruction) and
 // loads each add what the schedule does not hide.  256 x 256 tiles read least
