@@ -417,9 +417,9 @@ rs_status reshard_moe_route(const rs_router* router, int64_t n_tokens, const voi
  * is an empty slot.  The same formulas as the forward pass hold, over the
  * slots given: NaN and -infinity logits have score and gradient 0, and
  * dweights of slots that name them, or no expert, is not used.  Gradients are
- * good to float32's rounding of their own magnitude; for softmax weights that
- * are not renormalised, whose formula is s_e * (dweights_e - sum of dweights *
- * s), to the rounding of s_e times the largest dweights. */
+ * good to float32's rounding of scale * s_e (1 - s_e) times the largest
+ * |dweights| (s_e being the share of the sum where renormalise is 1), so a
+ * score next to 1 keeps its digits as one next to 0 does. */
 rs_status reshard_moe_route_grad(const rs_router* router, int64_t n_tokens, const void* logits,
                                  int64_t logits_stride, const int32_t* ids, const float* dweights,
                                  void* dlogits, int64_t dlogits_stride, void* stream);

@@ -524,7 +524,10 @@ __global__ __launch_bounds__(256) void rs_route_kernel(RouteArgs p) {
 // for the sigmoid, H_e being the sum of g_j over the slots that name e.
 // Renormalised weights, with their shares r_j = p_j / sum p: dl_e is the sum of
 // r_j (g_j - sum g r) over the slots that name e (the softmax's sum over all
-// slots is 0), times 1 - s_e for the sigmoid.  Sixteen lanes a token, a run of
+// slots is 0), times 1 - s_e for the sigmoid.  The expert with the largest
+// score, whose own part of such a sum may be next to all of it, takes the
+// others' instead: H_e (1 - s_e) - sum over the others, 1 - s_e being their
+// scores' sum.  Sixteen lanes a token, a run of
 // experts and one or two slots a lane; H (what is not the softmax's own, with
 // its factors: dl_e itself) goes through LDS, each expert written by the first
 // slot that names it with the sum of all that do, in slot order.
@@ -550,7 +553,7 @@ __global__ __launch_bounds__(RUN > 16 ? 64 : 256) void rs_route_grad_kernel(Rout
   const int first = lane * p.run;
   const int held = live ? max(0, min(p.run, p.n_experts - first)) : 0;
   float s[RUN];
-  float m = 0.0f, z = 1.0f;
+  float m = 0.0f, z = 1.0f, rest = 0.0f;  // rest: what a score above a half leaves to the others
   if (!p.sigmoid) {
     float x[RUN];
     load_run<RUN>(p.logits, p.dtype, row + first, held, x);
@@ -568,7 +571,11 @@ __global__ __launch_bounds__(RUN > 16 ? 64 : 256) void rs_route_grad_kernel(Rout
     z = row_sum16f(z);
     const float rz = z > 0.0f ? 1.0f / z : 0.0f;
 #pragma unroll
-    for (int j = 0; j < RUN; ++j) s[j] *= rz;
+    for (int j = 0; j < RUN; ++j) {
+      s[j] *= rz;
+      rest += s[j] > 0.5f ? 0.0f : s[j];
+    }
+    rest = row_sum16f(rest);
     z = rz;
   }
   int32_t id[2];
@@ -583,22 +590,31 @@ __global__ __launch_bounds__(RUN > 16 ? 64 : 256) void rs_route_grad_kernel(Rout
     // a score that is 0 for good takes no gradient, whatever dweights holds there
     h[a] = l[a] > -INFINITY ? p.scale * p.dweights[t * p.top_k + i] : 0.0f;
   }
-  float mean = 0.0f;
+  float mean = 0.0f, others = 0.0f;
   if (p.renormalise) {
-    const Share base = share_base(row_max16f(fmaxf(l[0], l[1])), m, p.sigmoid);
+    const float top = row_max16f(fmaxf(l[0], l[1]));
+    const Share base = share_base(top, m, p.sigmoid);
+    const int first_of_all = int(row_max16u(max(l[0] == top ? uint32_t(id[0] + 1) : 0u, l[1] == top ? uint32_t(id[1] + 1) : 0u))) - 1;
 #pragma unroll
     for (int a = 0; a < 2; ++a) q[a] = share32(l[a], base, p.sigmoid);
     const float sum = row_sum16f(q[0] + q[1]);
 #pragma unroll
     for (int a = 0; a < 2; ++a) q[a] = sum > 0.0f ? q[a] / sum : 0.0f;
-    const float gr = row_sum16f(h[0] * q[0] + h[1] * q[1]);
+    const bool large[2] = {id[0] == first_of_all, id[1] == first_of_all};
+    const float left = row_sum16f((large[0] ? 0.0f : q[0]) + (large[1] ? 0.0f : q[1]));
+    others = row_sum16f((large[0] ? 0.0f : h[0] * q[0]) + (large[1] ? 0.0f : h[1] * q[1]));
+    mean = others + row_sum16f((large[0] ? h[0] * q[0] : 0.0f) + (large[1] ? h[1] * q[1] : 0.0f));
 #pragma unroll
-    for (int a = 0; a < 2; ++a) h[a] = q[a] * (h[a] - gr);
+    for (int a = 0; a < 2; ++a) h[a] = q[a] * (large[a] ? h[a] * left - others : h[a] - mean);
   } else {
 #pragma unroll
     for (int a = 0; a < 2; ++a) q[a] = score32(l[a], m, z, p.sigmoid);
-    if (!p.sigmoid) mean = row_sum16f(h[0] * q[0] + h[1] * q[1]);
-    else h[0] *= q[0], h[1] *= q[1];
+    if (!p.sigmoid) {
+      mean = row_sum16f(h[0] * q[0] + h[1] * q[1]);
+      others = row_sum16f((q[0] > 0.5f ? 0.0f : h[0] * q[0]) + (q[1] > 0.5f ? 0.0f : h[1] * q[1]));
+    } else {
+      h[0] *= q[0], h[1] *= q[1];
+    }
   }
   if (p.sigmoid) {
 #pragma unroll
@@ -628,7 +644,8 @@ __global__ __launch_bounds__(RUN > 16 ? 64 : 256) void rs_route_grad_kernel(Rout
 #pragma unroll
   for (int j = 0; j < RUN; ++j) {
     const float H = mine[lane * RUN + j];
-    s[j] = p.sigmoid || p.renormalise ? H : s[j] > 0.0f ? s[j] * (H - mean) : 0.0f;
+    const float d = s[j] > 0.5f ? H * rest - others : H - mean;
+    s[j] = p.sigmoid || p.renormalise ? H : s[j] > 0.0f ? s[j] * d : 0.0f;
   }
   const int64_t to = t * p.dstride + first;
   if (RUN % 8 == 0 && held == RUN) {

@@ -540,3 +540,55 @@ def test_route_where_the_sum_of_exponentials_rounds_one_way(E, G):
         bias[0] = -0.99
         bias[other] = float(np.float32(s + float(bias[0]) - gap * H.U))
         check_route(x.cuda(), dict(k=2, score="softmax", renorm=False, groups=G, top_groups=1), bias.cuda())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E,k", [(16, 3), (128, 8), (1000, 20)])
+def test_route_grad_of_a_score_next_to_one(score, renorm, E, k):
+    """One expert far above the others: its own entry, s (1 - s) of the
+    differences, keeps its digits.  Per expert, the scores are off as in
+    H.route_grad; H (1 - s) - sum of the others' counts 3 U of each magnitude
+    for the top one, H - sum of all three times what is left of it for the
+    others (1 - s is a half there at the least)."""
+    g = torch.Generator().manual_seed(E)
+    x = torch.randn(12, E, generator=g) - (40 if score == "sigmoid" and renorm else 0)
+    at = torch.arange(12) % E
+    for t, gap in enumerate((0.5, 2, 5, 8, 10, 12, 14, 16, 18, 20, 25, 30)):
+        x[t, at[t]] = x[t].max() + gap
+    rng = np.random.default_rng(k)
+    ids = np.stack([np.concatenate([[at[t]], rng.permutation(np.delete(np.arange(E), at[t]))[:k - 1]]) for t in range(12)]).astype(np.int32)
+    ids = np.ascontiguousarray(np.take_along_axis(ids, np.argsort(rng.random(ids.shape), 1), 1))
+    dw = rng.normal(0, 1, (12, k)).astype(np.float32)
+    if k > 8:
+        ids[::3, 0] = ids[::3, 1] = at[::3].numpy()   # named twice or more
+    r = B.Router("f32", E, k, score=score, renormalise=renorm, scale=1.5)
+    out = torch.full((12, E), 7.0, device="cuda")
+    B.reshard_moe_route_grad(r, 12, ptr(x.cuda()), E, ptr(torch.from_numpy(ids).cuda()), ptr(torch.from_numpy(dw).cuda()), ptr(out), E, stream())
+    s, d = H.scores(f64(x), score)
+    want, tol = np.zeros((12, E)), np.zeros((12, E))
+    for t in range(12):
+        h, c = np.zeros(E), np.zeros(E)   # sums of dweights and of their magnitudes by expert, slots by expert
+        a = np.zeros(E)
+        for j in range(k):
+            h[ids[t, j]] += 1.5 * dw[t, j]
+            a[ids[t, j]] += 1.5 * abs(float(dw[t, j]))
+            c[ids[t, j]] += 1
+        if renorm:     # shares of the sum over the slots: sum_e c_e r_e = 1
+            p = s[t] * (c > 0)
+            w = p / (p * c).sum()
+        else:
+            w, c = s[t], np.ones(E)
+        if not renorm and score == "sigmoid":
+            e = np.exp(-np.abs(f64(x[t])))
+            want[t], tol[t] = e / (1 + e) ** 2 * h, e / (1 + e) ** 2 * a * 24 * H.U
+            continue
+        # sum_f w_f (c_f h_e - c_e h_f), without cancellation of the part that e itself has
+        diff, mag = np.zeros(E), np.zeros(E)
+        for i in range(E):
+            o = np.arange(E) != i
+            diff[i] = h[i] * (w * c)[o].sum() - c[i] * (w * h)[o].sum()
+            mag[i] = a[i] * (w * c)[o].sum() + c[i] * (w * a)[o].sum()
+        f = 1 / (1 + np.exp(f64(x[t]))) if score == "sigmoid" else 1.0
+        want[t], tol[t] = w * diff * f, w * mag * f * 3 * (2 * d[t] + 128 + k) * H.U
+    H.close(f64(out), want, tol, "f32", "dlogits")
