@@ -31,12 +31,13 @@ struct QuantArgs {
 
 // silu(gate) * up, by e = exp(-|gate|), which is at most 1: a gate below 0
 // gives gate * e / (1 + e), so that a sigmoid below 2^-126 loses no more than a
-// subnormal e does.  The reciprocal instruction's 2^-23 is refined once, to
+// subnormal e does.  Of gate and gate * e the larger is the one meant (of
+// infinities and NaN either marks the block).  The reciprocal instruction's 2^-23 is refined once, to
 // half a step: with exp (2^-23), the addition and three products below 7 steps
 // of 2^-24 in all.
 __device__ __forceinline__ float gated(float gate, float up) {
   const float e = expf(-fabsf(gate)), d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
-  return (gate < 0.0f ? gate * e : gate) * fmaf(fmaf(-d, r, 1.0f), r, r) * up;
+  return __builtin_amdgcn_fmed3f(gate, gate * e, INFINITY) * fmaf(fmaf(-d, r, 1.0f), r, r) * up;
 }
 
 __device__ __forceinline__ uint32_t amax_bits(const float v[8]) {
